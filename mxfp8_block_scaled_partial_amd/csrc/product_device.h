@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "layer_internal.h"
+#include "load_bounds.h"
 
 namespace mxfp8 {
 
@@ -45,15 +46,6 @@ struct ProductArgs {
   int tiles_m, tiles_n;
   uint8_t* packed;       // large tiles: the operands' scales, [2][group][row][16]
 };
-
-// Swizzle of a tile stored along the rows of its array; see each kernel's LDS layout.
-template <int T>
-__device__ constexpr int rows_swizzle(int k) {
-  constexpr int chunks = T / 16;
-  if constexpr (chunks == 12) return 2 * ((k >> 2) & 1);  // rows 48 banks apart: 4 of them cover all
-  constexpr int sh = chunks >= 16 ? 0 : chunks == 8 ? 1 : chunks == 4 ? 2 : 3;
-  return (2 * ((k & 7) >> sh)) & (chunks - 1);
-}
 
 // ---------------------------------------------------------------- scales
 //

@@ -45,13 +45,10 @@ __device__ inline void each(Body&& f) {
   }
 }
 
-
-constexpr int kHalf = 64;  // values of the sum per phase
-
-// One operand's loads.  LDS layout of a half: ALONG_COLS [T rows][4 chunks of 16], chunk c of row
-// r at position c ^ ((r >> 2) & 3); ALONG_ROWS [64 k][T / 16 chunks], chunk c of row k at
-// c ^ rows_swizzle(k).  16 lanes reading one chunk of 16 successive rows, or 8 rows of 2
-// neighbouring chunks, so touch every bank once.
+// One operand's loads; load_bounds.h has their addresses.  LDS layout of a half: ALONG_COLS [T
+// rows][4 chunks of 16], chunk c of row r at position c ^ ((r >> 2) & 3); ALONG_ROWS [64 k][T / 16
+// chunks], chunk c of row k at c ^ rows_swizzle(k).  16 lanes reading one chunk of 16 successive
+// rows, or 8 rows of 2 neighbouring chunks, so touch every bank once.
 template <int T, bool kRows>
 struct Stream {
   static constexpr int kLoads = T / 64;  // 16-byte loads of a thread per half
@@ -59,23 +56,15 @@ struct Stream {
   uint32_t off[kLoads];  // of the thread's chunks from the half's base
   int kk;                // ALONG_COLS: where they lie in the half
   const uint8_t* base;
-  uint32_t extent;       // ALONG_COLS: bytes of the tile's rows; ALONG_ROWS: of the last k's row
+  uint32_t extent;       // ALONG_COLS: bytes the loads may touch; ALONG_ROWS: columns from outer0 on
   int left;              // values of the sum from the half's start
 
   __device__ inline void init(const Operand& o, int tid) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int slot = i * 256 + tid;
-      if constexpr (kRows) {
-        constexpr int chunks = T / 16;
-        const int k = slot / chunks;
-        off[i] = (uint32_t)(k * (int)o.ld + 16 * ((slot % chunks) ^ rows_swizzle<T>(k)));
-        kk = 0;
-      } else {
-        const int r = slot / 4;
-        kk = 16 * ((slot % 4) ^ ((r >> 2) & 3));  // the same for every i
-        off[i] = (uint32_t)(r * (int)o.ld + kk);
-      }
+      const Place p = place_of<T, kRows>(i * 256 + tid);
+      off[i] = (uint32_t)(p.row * (int)o.ld + p.at);
+      kk = kRows ? 0 : p.at;  // the same for every i
     }
   }
 
@@ -86,9 +75,8 @@ struct Stream {
       base = o.data + k0 * o.ld + outer0;
       extent = (uint32_t)(o.outer - outer0);
     } else {
-      const int64_t rows = o.outer - outer0 < T ? o.outer - outer0 : T;
       base = o.data + outer0 * o.ld + k0;
-      extent = (uint32_t)((rows - 1) * o.ld + kHalf);
+      extent = cols_extent<T>(o.outer - outer0, o.ld);
     }
   }
   __device__ inline void finish() { left = 0; }  // nothing more: every load reads 0
@@ -96,8 +84,7 @@ struct Stream {
   // The half's buffer resource: lanes past the last row read 0.
   __device__ inline v4i resource(const Operand& o) const {
     const uint64_t b = (uint64_t)base;
-    uint32_t e = extent;
-    if constexpr (kRows) e = left > 0 ? (uint32_t)((min(left, kHalf) - 1) * (int)o.ld) + extent : 0;
+    const uint32_t e = kRows ? rows_extent(left, (int)o.ld, extent) : extent;
     return v4i{__builtin_amdgcn_readfirstlane((int)b),
                __builtin_amdgcn_readfirstlane((int)(b >> 32) & 0xFFFF),
                __builtin_amdgcn_readfirstlane((int)e), 0x00020000};
@@ -106,7 +93,7 @@ struct Stream {
   // Starts load i of the half into LDS at byte `lds` (the buffer plus 1 KB per wave).
   __device__ inline void load(int i, const v4i& rsrc, uint32_t lds) const {
     uint32_t o = off[i];
-    if constexpr (!kRows) o = kk < left ? o : 0xFFFFFFF0u;
+    if constexpr (!kRows) o = cols_offset(o, kk, left);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :: "s"(lds + i * 4096), "v"(o), "s"(rsrc));
   }
