@@ -48,14 +48,15 @@ struct Args {
 };
 
 // s = 1 / (1 + exp(-x)) and c = 1 - s = exp(-x) s, each within a few units in the last place (c
-// without the cancellation of 1 - s); below -87.3, where s is under 2^-125, it is taken as 0.
+// without the cancellation of 1 - s); below -87.3, where s is under 2^-125, it is taken as 0.  Far
+// on the other side c has to reach 0 too: x may be as large as FP32 holds, and x c counts.
 struct Sigmoid {
   float s, c;
 };
 __device__ inline Sigmoid sigmoid(float x) {
   // exp(-x) = 2^t, t = -x log2 e in two parts so that large |x| keeps its relative accuracy
   constexpr float kHi = -1.44269504f, kLo = -1.92596299e-8f;
-  const float xc = fminf(fmaxf(x, -87.3f), 87.3f);  // 2^t stays finite and normal
+  const float xc = fminf(fmaxf(x, -87.3f), 150.f);  // 2^t stays finite, and from there on is 0
   const float t = xc * kHi;
   const float r = __builtin_fmaf(xc, kHi, -t) + xc * kLo;
   const float p = __builtin_amdgcn_exp2f(t);
