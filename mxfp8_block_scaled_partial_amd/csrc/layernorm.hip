@@ -1,8 +1,10 @@
 // Layer norm forward and backward (mxfp8_layernorm_forward, mxfp8_layernorm_backward) on
 // gfx950.
 //
-// forward:  mean and variance of each row in FP32, the variance from the deviations (a second
-//           pass over the row's values), then y = (x - mean) rstd gamma + beta.
+// forward:  mean and variance of each row in FP32: a first mean m, then the sums of d = x - m and
+//           d^2 (a second pass over the row's values), which correct it: mean = m + mean(d),
+//           variance = mean(d^2) - mean(d)^2, y = (d - mean(d)) rstd gamma + beta.  The rounding of
+//           m, which counts where a row's mean is far above its deviation, so leaves no trace.
 // backward: with xh = (x - mean) rstd and g = gamma dy,
 //           dx = rstd (g - mean(g) - xh mean(g xh)), dgamma = sum dy xh, dbeta = sum dy.
 // Bound by HBM: 2 and 3 passes over rows x cols values.  A row stays in registers between its
@@ -75,9 +77,27 @@ __device__ inline float2 block_sum2(float a, float b, float2* scratch) {
   return s;
 }
 
+// A first mean, rounded to FP32 here: without this the compiler subtracts the unrounded product from
+// the values, and `off` would belong to another mean than the one it is added to.
+__device__ inline float first_mean(float sum, float inv) {
+  float mean = sum * inv;
+  asm("" : "+v"(mean));
+  return mean;
+}
+
+__device__ inline bool finite(float x) { return fabsf(x) < __builtin_inff(); }
+
+// 1 / sqrt(variance + eps) from the mean square of the deviations from a value that is `off` below
+// the mean.  Rounding may take a variance of 0 below it; an infinity or NaN stays one.
+__device__ inline float rstd_of(float square, float off, float eps) {
+  const float var = finite(square) ? fmaxf(square - off * off, 0.f) : square;
+  return 1.f / sqrtf(var + eps);
+}
+
 template <bool kBF16, int kThreads, int kVec>
 __global__ __launch_bounds__(kThreads) void forward_row_kernel(const Args g) {
-  __shared__ float scratch[2][kThreads / 64];
+  __shared__ float scratch[kThreads / 64];
+  __shared__ float2 scratch2[kThreads / 64];
   const float inv = 1.f / (float)g.cols;
   for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
     Raw<kBF16> raw[kVec];
@@ -93,8 +113,8 @@ __global__ __launch_bounds__(kThreads) void forward_row_kernel(const Args g) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += x.v[e];
     }
-    const float mean = block_sum<kThreads>(s, scratch[0]) * inv;
-    s = 0.f;
+    const float mean = first_mean(block_sum<kThreads>(s, scratch), inv);
+    float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const int64_t n = g.cols - 8 * (int64_t)(i * kThreads + threadIdx.x);
@@ -102,11 +122,12 @@ __global__ __launch_bounds__(kThreads) void forward_row_kernel(const Args g) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float d = e < n ? x.v[e] - mean : 0.f;
-        s += d * d;
+        s1 += d;
+        s2 += d * d;
       }
     }
-    const float var = block_sum<kThreads>(s, scratch[1]) * inv;
-    const float rstd = 1.f / sqrtf(var + g.eps);
+    const float2 t = block_sum2<kThreads>(s1, s2, scratch2);
+    const float off = t.x * inv, rstd = rstd_of(t.y * inv, off, g.eps);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const int64_t c = 8 * (int64_t)(i * kThreads + threadIdx.x), n = g.cols - c;
@@ -117,11 +138,11 @@ __global__ __launch_bounds__(kThreads) void forward_row_kernel(const Args g) {
       if (g.gamma) ga = load8<false>(g.gamma, c, n);
       if (g.beta) be = load8<false>(g.beta, c, n);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x.v[e] = (x.v[e] - mean) * rstd * ga.v[e] + be.v[e];
+      for (int e = 0; e < 8; ++e) x.v[e] = (x.v[e] - mean - off) * rstd * ga.v[e] + be.v[e];
       store8<kBF16>(g.y, r * g.ldy + c, n, x);
     }
     if (threadIdx.x == 0) {
-      if (g.mean) g.mean[r] = mean;
+      if (g.mean) g.mean[r] = finite(mean) ? mean + off : mean;
       if (g.rstd) g.rstd[r] = rstd;
     }
   }
@@ -208,30 +229,46 @@ __global__ __launch_bounds__(kThreads) void backward_group_kernel(const Args g) 
 
 // ---- rows too wide for the registers
 
+// A compensated sum: the rounding of each addition is carried into the next, so a thread's sum is as
+// exact over millions of columns as over a few.  Infinities and NaN sum as they do in plain additions.
+struct Sum {
+  float s = 0.f, c = 0.f;
+  __device__ inline void add(float v) {
+    const float y = v - c, t = s + y;
+    c = finite(t) ? (t - s) - y : 0.f;
+    s = t;
+  }
+  // 8 values, joined in a tree first
+  __device__ inline void add(const float (&v)[8]) {
+    add(((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])));
+  }
+};
+
 template <bool kBF16>
 __global__ __launch_bounds__(256) void forward_kernel(const Args g) {
   __shared__ float scratch[4];
+  __shared__ float2 scratch2[4];
   const float inv = 1.f / (float)g.cols;
   for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
     const int64_t base = r * g.ldx;
-    float s = 0.f;
+    Sum s;
+    for (int64_t c = 8 * threadIdx.x; c < g.cols; c += 2048)
+      s.add(load8<kBF16>(g.x, base + c, g.cols - c).v);
+    const float mean = first_mean(block_sum<256>(s.s, scratch), inv);
+    Sum s1, s2;
     for (int64_t c = 8 * threadIdx.x; c < g.cols; c += 2048) {
       const Chunk x = load8<kBF16>(g.x, base + c, g.cols - c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += x.v[i];
-    }
-    const float mean = block_sum<256>(s, scratch) * inv;
-    s = 0.f;
-    for (int64_t c = 8 * threadIdx.x; c < g.cols; c += 2048) {
-      const Chunk x = load8<kBF16>(g.x, base + c, g.cols - c);
+      float d[8], q[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = c + i < g.cols ? x.v[i] - mean : 0.f;
-        s += d * d;
+        d[i] = c + i < g.cols ? x.v[i] - mean : 0.f;
+        q[i] = d[i] * d[i];
       }
+      s1.add(d);
+      s2.add(q);
     }
-    const float var = block_sum<256>(s, scratch) * inv;
-    const float rstd = 1.f / sqrtf(var + g.eps);
+    const float2 t = block_sum2<256>(s1.s, s2.s, scratch2);
+    const float off = t.x * inv, rstd = rstd_of(t.y * inv, off, g.eps);
     for (int64_t c = 8 * threadIdx.x; c < g.cols; c += 2048) {
       const int64_t n = g.cols - c;
       Chunk x = load8<kBF16>(g.x, base + c, n), ga, be;
@@ -240,11 +277,11 @@ __global__ __launch_bounds__(256) void forward_kernel(const Args g) {
       if (g.gamma) ga = load8<false>(g.gamma, c, n);
       if (g.beta) be = load8<false>(g.beta, c, n);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x.v[i] = (x.v[i] - mean) * rstd * ga.v[i] + be.v[i];
+      for (int i = 0; i < 8; ++i) x.v[i] = (x.v[i] - mean - off) * rstd * ga.v[i] + be.v[i];
       store8<kBF16>(g.y, r * g.ldy + c, n, x);
     }
     if (threadIdx.x == 0) {
-      if (g.mean) g.mean[r] = mean;
+      if (g.mean) g.mean[r] = finite(mean) ? mean + off : mean;
       if (g.rstd) g.rstd[r] = rstd;
     }
   }
@@ -256,7 +293,7 @@ __global__ __launch_bounds__(256) void backward_rows_kernel(const Args g) {
   const float inv = 1.f / (float)g.cols;
   for (int64_t r = blockIdx.x; r < g.rows; r += gridDim.x) {
     const float mean = g.mean[r], rstd = g.rstd[r];
-    float s1 = 0.f, s2 = 0.f;
+    Sum s1, s2;
     for (int64_t c = 8 * threadIdx.x; c < g.cols; c += 2048) {
       const int64_t n = g.cols - c;
       const Chunk x = load8<kBF16>(g.x, r * g.ldx + c, n), d = load8<kBF16>(g.dy, r * g.lddy + c, n);
@@ -264,15 +301,17 @@ __global__ __launch_bounds__(256) void backward_rows_kernel(const Args g) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) ga.v[i] = 1.f;
       if (g.gamma) ga = load8<false>(g.gamma, c, n);
+      float gd[8], gx[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float gd = ga.v[i] * d.v[i];
-        s1 += gd;
-        s2 += gd * ((x.v[i] - mean) * rstd);
+        gd[i] = ga.v[i] * d.v[i];
+        gx[i] = gd[i] * ((x.v[i] - mean) * rstd);
       }
+      s1.add(gd);
+      s2.add(gx);
     }
-    const float m1 = block_sum<256>(s1, scratch) * inv;
-    const float m2 = block_sum<256>(s2, scratch) * inv;
+    const float m1 = block_sum<256>(s1.s, scratch) * inv;
+    const float m2 = block_sum<256>(s2.s, scratch) * inv;
     for (int64_t c = 8 * threadIdx.x; c < g.cols; c += 2048) {
       const int64_t n = g.cols - c;
       const Chunk x = load8<kBF16>(g.x, r * g.ldx + c, n);
