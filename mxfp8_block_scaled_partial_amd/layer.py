@@ -9,7 +9,7 @@ workspace, so they have to be ordered like any calls that share buffers.  There 
 fallback.
 
 8-bit matrices are uint8 tensors (or ``torch.float8_e4m3fn`` / ``float8_e8m0fnu`` views) of E4M3
-codes and E8M0 scale bytes.
+codes and E8M0 scale bytes; tensors of any other type are refused.
 """
 from __future__ import annotations
 
@@ -24,6 +24,7 @@ ALONG_COLS, ALONG_ROWS = 0, 1
 ALONG = {"cols": ALONG_COLS, "rows": ALONG_ROWS}
 ACT_NONE, ACT_GELU, ACT_SWIGLU = range(3)
 ACT_FUNCS = {"none": ACT_NONE, "gelu": ACT_GELU, "swiglu": ACT_SWIGLU}
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 BLOCK = 128  # values that share a scale in the 8-bit matrices these operators write
 
 # every entry point declared in include/layer/mxfp8_layer.h
@@ -93,7 +94,7 @@ def lib():
 # ------------------------------------------------------------------ tensor marshalling
 
 
-def _matrix(t, rows, cols, what, dtype=None, esize=None) -> Buf:
+def _matrix(t, rows, cols, what, dtype=None) -> Buf:
     """A row-major [rows, cols] tensor with unit column stride; an absent one (None, or without
     elements) is an empty handle."""
     if not B._present(t):
@@ -102,8 +103,6 @@ def _matrix(t, rows, cols, what, dtype=None, esize=None) -> Buf:
         raise ValueError(f"{what} must be [{rows}, {cols}], got shape {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if esize is not None and t.element_size() != esize:
-        raise ValueError(f"{what} must hold {esize}-byte elements")
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{what} must have unit stride along its last dimension")
     ld = t.stride(0) if rows > 1 else cols
@@ -124,14 +123,22 @@ def _blocks(n: int, block: int) -> int:
     return (n + block - 1) // block
 
 
+def _bytes(t, kind, what):
+    """Refuses an 8-bit tensor of another format, whose bytes would be read as this one's."""
+    if t is not None and t.dtype not in (torch.uint8, kind):
+        raise ValueError(f"{what} must be uint8 or {kind}, got {t.dtype}")
+
+
 def _mat8(pair, rows, cols, by_cols, what) -> Mat8:
     """A (data, scale) pair in row-wise or column-wise blocks of 128; None is absent."""
     if pair is None:
         return Mat8(None, 0, None, 0)
     data, scale = pair
-    d = _matrix(data, rows, cols, f"{what} data", esize=1)
+    _bytes(data, E4M3, f"{what} data")
+    _bytes(scale, E8M0, f"{what} scale")
+    d = _matrix(data, rows, cols, f"{what} data")
     s = _matrix(scale, _blocks(rows, BLOCK) if by_cols else rows,
-                cols if by_cols else _blocks(cols, BLOCK), f"{what} scale", esize=1)
+                cols if by_cols else _blocks(cols, BLOCK), f"{what} scale")
     return Mat8(d.ptr, d.ld, s.ptr, s.ld)
 
 
@@ -165,14 +172,16 @@ def make_operand(data, scale, *, along: str = "cols", block: int = BLOCK,
         raise ValueError(f"along must be 'cols' or 'rows', got {along!r}")
     if block not in (32, 128) or across not in (1, 128):
         raise ValueError(f"block must be 32 or 128 and across 1 or 128, got {block}, {across}")
+    _bytes(data, E4M3, "data")
+    _bytes(scale, E8M0, "scale")
     if data.dim() != 2:
         raise ValueError(f"data must be 2-D, got shape {tuple(data.shape)}")
-    d = _matrix(data, data.shape[0], data.shape[1], "data", esize=1)
+    d = _matrix(data, data.shape[0], data.shape[1], "data")
     sr, sc = (across, block) if along == "cols" else (block, across)
     rows, cols = _blocks(data.shape[0], sr), _blocks(data.shape[1], sc)
     if scale.dim() != 2 or scale.shape[0] < rows or scale.shape[1] < cols:
         raise ValueError(f"scale shape {tuple(scale.shape)} is smaller than [{rows}, {cols}]")
-    s = _matrix(scale[:rows, :cols], rows, cols, "scale", esize=1)
+    s = _matrix(scale[:rows, :cols], rows, cols, "scale")
     o = Operand(d.ptr, d.ld, s.ptr, s.ld, ALONG[along], block, across, 0)
     o.outer, o.k = (data.shape if along == "cols" else data.shape[::-1])
     o.tensors = (data, scale)
