@@ -109,9 +109,15 @@ class FeedForward:
                 dbeta=self.dbeta, eps=eps)),
         ]
 
+    def _take(self, buffer, values, what):
+        """Copies a step's values into the layer's buffer, which a broadcast would fill with others."""
+        if values.shape != buffer.shape:
+            raise ValueError(f"{what} must be {list(buffer.shape)}, got {list(values.shape)}")
+        buffer.copy_(values)
+
     def forward(self, x) -> torch.Tensor:
-        """y [tokens, features] bfloat16 (the layer's own buffer) of x."""
-        self.x.copy_(x)
+        """y [tokens, features] bfloat16 (the layer's own buffer) of x [tokens, features]."""
+        self._take(self.x, x, "x")
         for call, plan in self._forward:
             call(plan)
         return self.y
@@ -120,7 +126,7 @@ class FeedForward:
         """The gradient of x (the layer's own buffer) for the last forward pass."""
         if self._backward is None:
             raise ValueError("the layer was planned without training")
-        self.dy.copy_(dy)
+        self._take(self.dy, dy, "dy")
         for call, plan in self._backward:
             call(plan)
         return self.dx
