@@ -38,7 +38,9 @@ class FeedForward:
     ``weight_specs(features, hidden)`` with full-size storage; later updates of it change the
     weights this layer reads.  ``gamma`` and ``beta`` are float32 vectors.
 
-    ``backward`` adds to ``grads`` (float32): gate, up, down; and fills dgamma and dbeta."""
+    ``backward`` adds to ``grads`` (float32): gate, up, down; and fills dgamma and dbeta.  The layer
+    is no node of autograd: it takes the values of tensors that require gradients, and its outputs
+    require none."""
 
     def __init__(self, writeback: W.Writeback, gamma, beta, tokens: int, *, eps: float = 1e-5,
                  training: bool = True):
@@ -110,10 +112,11 @@ class FeedForward:
         ]
 
     def _take(self, buffer, values, what):
-        """Copies a step's values into the layer's buffer, which a broadcast would fill with others."""
+        """Copies a step's values into the layer's buffer, which a broadcast would fill with others and
+        a copy of a tensor with a graph would hang on that graph."""
         if values.shape != buffer.shape:
             raise ValueError(f"{what} must be {list(buffer.shape)}, got {list(values.shape)}")
-        buffer.copy_(values)
+        buffer.copy_(values.detach())
 
     def forward(self, x) -> torch.Tensor:
         """y [tokens, features] bfloat16 (the layer's own buffer) of x [tokens, features]."""

@@ -17,3 +17,19 @@ def test_inputs_of_another_shape_are_refused():
             ff.forward(bad)
         with pytest.raises(ValueError, match=r"\[12, 256\]"):
             ff.backward(bad)
+
+
+def test_inputs_that_require_gradients():
+    """The layer's buffers stay plain storage: no graph hangs on them from step to step, and the
+    results are those of the same values without a graph."""
+    wb, gamma, beta, ff, g = build(256, 384, 12, 2)
+    x = torch.randn(12, 256, generator=g, device=DEV).to(torch.bfloat16)
+    want, dx = ff.forward(x).clone(), ff.backward(x).clone()
+    leaf = x.clone().requires_grad_()
+    for _ in range(2):
+        y = ff.forward(leaf * 1.0)
+        assert not y.requires_grad and not ff.x.requires_grad and ff.x.grad_fn is None
+        assert torch.equal(y, want)
+        got = ff.backward(leaf * 1.0)
+        assert not got.requires_grad and ff.dy.grad_fn is None
+        assert torch.equal(got, dx)
