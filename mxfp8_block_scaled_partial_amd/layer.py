@@ -148,12 +148,25 @@ def _workspace(need: int, workspace, device, struct):
         raise Mxfp8Error(-need, B.mxfp8_last_error())
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        struct.own = workspace, {B._stream(None)}
     if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         struct.workspace = B._dev_ptr(workspace, "workspace")
         struct.workspace_bytes = workspace.numel() * workspace.element_size()
     return workspace
+
+
+def _stream_of(struct, stream) -> int:
+    """The call's stream.  A workspace that the description made belongs to the stream that was
+    current then; the allocator learns of every other one that uses it, so that the memory is not
+    given away while such a call still runs after the description is gone."""
+    handle = B._stream(stream)
+    workspace, known = getattr(struct, "own", (None, ()))
+    if workspace is not None and handle not in known:
+        workspace.record_stream(torch.cuda.ExternalStream(handle, device=workspace.device))
+        known.add(handle)
+    return handle
 
 
 # ------------------------------------------------------------------ matrix product
@@ -209,7 +222,7 @@ def mxfp8_matmul_workspace(product: Product) -> int:
 
 
 def mxfp8_matmul(product: Product, stream=None) -> None:
-    B._check(lib().mxfp8_matmul(ctypes.byref(product), B._stream(stream)))
+    B._check(lib().mxfp8_matmul(ctypes.byref(product), _stream_of(product, stream)))
 
 
 # ------------------------------------------------------- activation with 8-bit checkpoint
@@ -292,4 +305,4 @@ def mxfp8_layernorm_forward(norm: LayerNorm, stream=None) -> None:
 
 
 def mxfp8_layernorm_backward(norm: LayerNorm, stream=None) -> None:
-    B._check(lib().mxfp8_layernorm_backward(ctypes.byref(norm), B._stream(stream)))
+    B._check(lib().mxfp8_layernorm_backward(ctypes.byref(norm), _stream_of(norm, stream)))

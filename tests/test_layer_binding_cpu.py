@@ -3,6 +3,7 @@ the library's validation."""
 import pytest
 import torch
 
+from mxfp8_block_scaled_partial_amd import binding as B
 from mxfp8_block_scaled_partial_amd import layer as L
 
 OTHERS = [torch.int8, torch.bool, torch.float8_e5m2, torch.float8_e4m3fnuz, torch.int16, torch.float32]
@@ -35,3 +36,43 @@ def test_views_of_the_right_format_are_taken():
                 L.make_operand(d, s)
             with pytest.raises(ValueError, match="device tensor"):
                 L._mat8((d, s), 64, 256, False, "row[0]")
+
+
+def test_own_workspace_on_another_stream(monkeypatch):
+    """The allocator is told, once, of every stream but the workspace's own that a call uses it on; a
+    caller's workspace is the caller's to keep."""
+    class Library:
+        mxfp8_matmul_workspace = mxfp8_layernorm_workspace = staticmethod(lambda p: 64)
+        mxfp8_matmul = mxfp8_layernorm_backward = staticmethod(lambda p, stream: 0)
+
+    current, told = [7], []
+    monkeypatch.setattr(L, "lib", Library)
+    monkeypatch.setattr(B, "_dev_ptr", lambda t, what: None if t is None else 4096)
+    monkeypatch.setattr(B, "_stream", lambda s: current[0] if s is None else s)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: handle)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: told.append((t.numel(), s)))
+    codes, scale = torch.zeros(8, 128, dtype=torch.uint8), torch.zeros(8, 1, dtype=torch.uint8)
+    v = torch.zeros(8)
+
+    def product(**kw):
+        return L.make_product(L.make_operand(codes, scale), L.make_operand(codes, scale), torch.zeros(8, 8), **kw)
+
+    def norm(**kw):
+        x = torch.zeros(8, 8)
+        return L.make_layernorm(x, mean=v, rstd=v, dy=x, dgamma=v, **kw)
+
+    for make, call in ((product, L.mxfp8_matmul), (norm, L.mxfp8_layernorm_backward)):
+        told.clear()
+        p = make()
+        call(p)
+        assert told == []
+        call(p, stream=9)
+        call(p, stream=9)
+        call(p, stream=7)
+        assert told == [(64, 9)]
+        current[0] = 11  # another current stream
+        call(p)
+        current[0] = 7
+        assert told == [(64, 9), (64, 11)]
+        call(make(workspace=torch.zeros(64, dtype=torch.uint8)), stream=9)
+        assert len(told) == 2
