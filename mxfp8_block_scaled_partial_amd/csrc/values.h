@@ -11,8 +11,6 @@ struct Chunk {
   float v[8];
 };
 
-__device__ inline float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
-
 __device__ inline uint32_t bf16_round(float x) {  // nearest even; NaN stays NaN
   return __builtin_bit_cast(uint16_t, (__bf16)x);
 }
