@@ -15,7 +15,10 @@
 // with this wave's loads of half t + 2 landed (the two phases' worth after them stay in flight)
 // and a barrier, so a load has two to three phases to land, 2048 to 3072 matrix cycles for
 // 256 x 256.  Two buffers of whole steps, whose loads fetch full 128-byte lines, leave it one to
-// two phases: 8192 x 14336 x 4096 took 515 us so, and 448 us with the ring.
+// two phases: 8192 x 14336 x 4096 took 515 us so, and 448 us with the ring
+// (the same inputs every call; the kernel as it is takes 443 us so, and 461 with inputs that change).  The 256 x 256 instances spill 20 to
+// 28 registers in BF16 and 66 to 112 in FP32, outside the main loop but for one: FP32 with only b
+// ALONG_ROWS reloads three in four half steps.
 //
 // The workgroups stay for all their tiles (one per CU), and the ring runs on from one tile into
 // the next: while a tile is stored, the first halves of the next land.
@@ -168,7 +171,8 @@ struct Out<true> {
 // rows of the wave's columns, 16 bytes a lane.  16-byte chunk c of staged row r lies at position
 // c ^ r (BF16) or c ^ 2 r (FP32): conflict-free both ways.  `add` is for FP32 only: a BF16 output
 // with an addend goes through FP32 partial sums and join_kernel, since code for it here costs
-// every BF16 tile registers (8192 x 14336 x 4096: 486 us instead of 444).
+// every BF16 tile registers (8192 x 14336 x 4096, the same inputs every call: 486 us
+// instead of 444).
 template <bool kF32, int kStage, int FM, int FN>
 __device__ inline void store_tile(v16f (&acc)[FM][FN], uint8_t* lds, int64_t m0, int64_t n0, int64_t m,
                                   int64_t n, void* out, int64_t ldo, const float* add,

@@ -7,10 +7,14 @@ The three weights are MXFP8 storage (row-wise and column-wise copies): forward p
 row-wise copies, the gradients of the inputs the column-wise ones.  Between the operators
 activations are 8-bit matrices in blocks of 128: row-wise for the next product, column-wise as
 the checkpoint that the weight gradients read; the gate's inputs are kept in 8 bits for its
-backward pass.  For a step of T tokens, C features and F hidden features the layer so keeps
+backward pass.  For a step of T tokens, C features and F hidden features the backward pass so reads
 T (C + 3 F) bytes of checkpoints beside x, where BF16 would take 2 T (C + 3 F).
 
-Everything is planned once for a number of tokens: buffers, workspaces and calls.
+Everything is planned once for a number of tokens: buffers, workspaces and calls.  A layer owns
+all of them, also those that hold nothing from the forward pass to the backward: beside the
+checkpoints and their scales that is T (7 C + 5 F) bytes of x, y, the norm's and the products'
+outputs and the 8-bit inputs of products, for training T (12 C + 6 F) more, and the products'
+workspaces.
 """
 from __future__ import annotations
 
